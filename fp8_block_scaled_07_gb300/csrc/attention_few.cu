@@ -707,6 +707,7 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
         if (!over) ok = mbar_wait(&qfull[sg & 1], (sg >> 1) & 1, abort_flag) && ok;
         const int least = s_min[sg & 1];
         float top_m = -INFINITY;       // the maximum of row lane % RU
+        bool settled = false;          // every row has one (the same in all threads)
         float ref[RU], l[RU];          // M - kPBits of each row (0 before there is one), the token's sums
 #pragma unroll
         for (int r = 0; r < RU; ++r) {
@@ -749,11 +750,14 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
                 for (int r = 0; r < RU; ++r) y[r] = -INFINITY;
             }
             // The maxima stay while every probability fits: then one barrier,
-            // which also says so, is all that the warps share of a tile.
+            // which also says so, is all that the warps share of a tile.  Not
+            // before every row has a maximum, though: one that has seen nothing
+            // so far (its tiles' pages are left out) has to get it with the
+            // first token that it sees, however small that one's exponent.
             float most = y[0];
 #pragma unroll
             for (int r = 1; r < RU; ++r) most = fmaxf(most, y[r]);
-            if (!bar_all(1, 128, ok && u > 0 && !(most > kMostBits))) {
+            if (!bar_all(1, 128, ok && settled && !(most > kMostBits))) {
                 // the true maxima: lane r of each warp gives its warp's, lane l
                 // of every warp then joins those of row l % RU
                 float mine = 0.0f;
@@ -773,6 +777,7 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
                 const bool grows = top > top_m;
                 const float my_fac = grows ? ex2(top_m - top) : 1.0f;   // 0 for the first
                 if (grows) top_m = top;
+                settled = __all_sync(0xFFFFFFFFu, top_m != -INFINITY) != 0;
                 float fac[RU];
 #pragma unroll
                 for (int r = 0; r < RU; ++r) {
