@@ -6,6 +6,7 @@ import torch
 
 import oracle
 from oracle import kv
+from tests.helpers import host_bits
 from tests.test_gpu_kv_attention import _case, _check, _run
 
 pytestmark = pytest.mark.gpu
