@@ -5,6 +5,8 @@
 #include "attention.cuh"
 
 namespace fp8bs {
+int take_debug_skip();   // gemm.cu
+
 namespace {
 
 bool block_size_ok(int32_t bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
@@ -72,6 +74,7 @@ extern "C" fp8_status fp8_kv_attention(const void* q, int64_t q_token_stride, in
     p.width = width;
     while ((1 << p.bs_log2) < block_size) ++p.bs_log2;
     p.scale = sm_scale * 1.4426950408889634f;
+    p.debug_skip = take_debug_skip();
     // The few-rows kernel reads a request's cache once for every ru rows, but
     // spreads it over the GPU; the many-rows kernel once for 256 rows, on one
     // SM for each of them and each cache head.  So a request stays with the

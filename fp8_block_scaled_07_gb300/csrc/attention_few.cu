@@ -384,9 +384,10 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
             __syncwarp();
             if (v.i < k.i && __all_sync(0xFFFFFFFFu, mbar_test(&vempty[v.i % SV], ((v.i / SV) & 1) ^ 1))) {
                 const int st = v.i % SV, np = pages(v.w);
-                if (lane == 0) mbar_arrive_expect_tx(&vfull[st], static_cast<uint32_t>(np * bs * DV));
+                const bool skip = p.debug_skip != 0 && v.i == 0 && me == 0;
+                if (lane == 0 && !skip) mbar_arrive_expect_tx(&vfull[st], static_cast<uint32_t>(np * bs * DV));
                 __syncwarp();
-                if (lane < np)
+                if (lane < np && !skip)
                     tma_load_page(sV + st * F::kVBytes + lane * bs * DV, &tm_v, &vfull[st], 0, v.w.h * bs / F::kPair, v.page);
                 advance(v);
                 moved = true;
@@ -699,7 +700,11 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
             done.last = -1;
             return good;
         };
-        for (int i = 0, sg = 0; ok && (i < ntiles || done.last >= 0); it.next_segment(), ++sg) {
+        // A wait that gave up in one thread only must not take that thread out:
+        // the others would wait at the next barrier for good.  All 128 leave
+        // together, on what a barrier says.
+        bool left = false;
+        for (int i = 0, sg = 0; i < ntiles || done.last >= 0; it.next_segment(), ++sg) {
         // ---- a segment, or what this range has of it; at the end a round without tiles
         const bool over = i >= ntiles;
         const int tile0 = it.tile, count = over ? 1 : min(it.nt - tile0, ntiles - i), len = it.len[it.b];
@@ -768,7 +773,10 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
                 }
                 if (lane < RU) s_max[w4 * RU + lane] = mine;
                 ok = bar_all(1, 128, ok);
-                if (!ok) break;
+                if (!ok) {
+                    left = true;
+                    break;
+                }
                 float top = s_max[lane % (4 * RU)];
 #pragma unroll
                 for (int k = 32; k < 4 * RU; k += 32) top = fmaxf(top, s_max[k + lane]);
@@ -845,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
             }
             if (u == 0 && done.last >= 0) ok = finish() && ok;
         }
-        if (!ok || over) break;
+        if (left || over) break;
 
         // ---- the segment's end: sums over the tokens
         int row = 0;

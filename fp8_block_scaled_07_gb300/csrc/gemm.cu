@@ -1761,10 +1761,12 @@ fp8_status decode_gemm(const void* x, const void* xq, const float* a_s, const vo
                        cudaStream_t st);
 bool decode_set_wait_limit(long long cycles);
 bool attention_set_wait_limit(long long cycles);   // attention.cu
+int take_debug_skip();
 }  // namespace fp8bs
 
 // Test hooks of the failure path (see fp8_debug_skip_one_arrive).
 static std::atomic<int> g_debug_skip_next{0};
+int fp8bs::take_debug_skip() { return g_debug_skip_next.exchange(0); }
 
 extern "C" fp8_status fp8_debug_set_wait_limit(long long cycles) {
     const long long v = cycles > 0 ? cycles : kWaitLimitCycles;

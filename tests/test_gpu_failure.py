@@ -85,3 +85,40 @@ def test_fused_gate_times_out_and_the_stream_recovers(fp8):
     assert _status(fp8) == 0
     assert torch.equal(gq.view(torch.uint8), yq.view(torch.uint8))
     assert torch.equal(gs.view(torch.int32), ys.view(torch.int32))
+
+
+# Attention over the paged cache: the first CTA's first tile of V does not come.  Few rows: requests of 40 tokens, so that
+# in each tile only the threads of the tokens past the length wait for V, and several requests to a CTA; heads of 64 have
+# one barrier more.  Prompts: V's conversion waits.
+@pytest.mark.parametrize("lens,new,Hq,Hkv,dk,dv", [([40] * 256, 1, 4, 4, 128, 128), ([40] * 256, 2, 8, 4, 64, 64),
+                                                   ([300] * 256, 1, 8, 4, 192, 128), ([300, 200], 150, 4, 2, 128, 128),
+                                                   ([700] * 40, 300, 4, 2, 64, 64)])
+def test_attention_without_a_tile_of_v_times_out_and_the_stream_recovers(fp8, lens, new, Hq, Hkv, dk, dv):
+    bs, B = 64, len(lens)
+    width = -(-max(lens) // bs)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    kc, ks, vc, vs = fp8.kv_cache(B * width, Hkv, bs, dk, dv)
+    for codes, scale in ((kc, ks), (vc, vs)):
+        codes.copy_(torch.randn(codes.shape, device="cuda", generator=gen).to(codes.dtype))
+        scale.fill_(1.0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    tables = torch.arange(B * width, **i32).view(B, width)
+    args = (torch.randn((B * new, Hq, dk), device="cuda", generator=gen).bfloat16(), kc, ks, vc, vs, tables,
+            torch.tensor(lens, **i32))
+    kw = dict(offsets=torch.arange(0, B * new + 1, new, **i32) if new > 1 else None, want_lse=True)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    want, wl = fp8.fp8_kv_attention(*args, workspace=ws, **kw)
+    assert _status(fp8) == 0
+    assert fp8.lib.fp8_debug_set_wait_limit(2_000_000) == 0
+    try:
+        fp8.lib.fp8_debug_skip_one_arrive()
+        fp8.fp8_kv_attention(*args, workspace=ws, **kw)
+        assert _status(fp8) == FP8_ERR_TIMEOUT
+        assert _status(fp8) == 0
+    finally:
+        torch.cuda.synchronize()
+        assert fp8.lib.fp8_debug_set_wait_limit(0) == 0
+    ws.zero_()   # what a workspace holds after a timeout is unspecified
+    out, lse = fp8.fp8_kv_attention(*args, workspace=ws, **kw)
+    assert _status(fp8) == 0
+    assert torch.equal(out, want) and torch.equal(lse, wl)
