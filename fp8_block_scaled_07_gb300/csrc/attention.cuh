@@ -55,7 +55,7 @@ struct AttnParams {
     int32_t B, Hq, Hkv, G, width, bs_log2;
     int32_t few_rows;    // requests of at most this many rows (queries x heads per cache head) are the few-rows kernel's
     int32_t fill_tail;   // this launch writes the rows past offsets[B]
-    int32_t debug_skip;  // test hook: the first CTA's first tile of V is never loaded
+    int32_t debug_skip;  // test hook: a CTA's first tile of V is never loaded
     float scale;         // sm_scale * log2(e)
 };
 

@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
             __syncwarp();
             if (v.i < k.i && __all_sync(0xFFFFFFFFu, mbar_test(&vempty[v.i % SV], ((v.i / SV) & 1) ^ 1))) {
                 const int st = v.i % SV, np = pages(v.w);
-                const bool skip = p.debug_skip != 0 && v.i == 0 && me == 0;
+                const bool skip = p.debug_skip != 0 && v.i == 0;
                 if (lane == 0 && !skip) mbar_arrive_expect_tx(&vfull[st], static_cast<uint32_t>(np * bs * DV));
                 __syncwarp();
                 if (lane < np && !skip)
@@ -964,7 +964,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
 #pragma unroll
     for (int e = 0; e < kV; ++e) s_o[warp][lane * kV + e] = o[e];
     __syncthreads();
-    if (share != 0 || at < 0) return;
+    // (after a wait that gave up, the record may be another call's)
+    if (share != 0 || at < 0 || at >= p.T * p.Hq) return;
 #pragma unroll
     for (int k = 1; k < kSplit; ++k) {
         float v[kV];

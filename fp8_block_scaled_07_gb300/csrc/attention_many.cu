@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 {
                     const int st = g % SV;
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&vempty[st], ((g / SV) & 1) ^ 1, abort_flag)) != 0;
-                    const bool skip = p.debug_skip != 0 && g == 0 && blockIdx.x == 0;
+                    const bool skip = p.debug_skip != 0 && g == 0;
                     if (lane == 0 && !skip) mbar_arrive_expect_tx(&vfull[st], static_cast<uint32_t>(np * bs * DV));
                     __syncwarp();
                     if (lane < np && !skip)

@@ -352,9 +352,8 @@ fp8_status fp8_device_status(void* stream);
  * epilogue: the epilogue's wait runs out, the kernel winds down (waits for
  * its own copies and MMAs, frees its tensor memory, returns) and
  * fp8_device_status then reports FP8_ERR_TIMEOUT; that call's output is
- * unspecified.  Where the next call is an fp8_kv_attention, the first CTA's
- * first tile of V is never loaded, in either of its kernels, with the same
- * end.  Neither is meant for production use. */
+ * unspecified.  Where the next call is an fp8_kv_attention, no CTA loads its
+ * first tile of V, in either of its kernels, with the same end.  Neither is meant for production use. */
 fp8_status fp8_debug_set_wait_limit(long long cycles);
 void fp8_debug_skip_one_arrive(void);
 

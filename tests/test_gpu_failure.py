@@ -87,7 +87,7 @@ def test_fused_gate_times_out_and_the_stream_recovers(fp8):
     assert torch.equal(gs.view(torch.int32), ys.view(torch.int32))
 
 
-# Attention over the paged cache: the first CTA's first tile of V does not come.  Few rows: requests of 40 tokens, so that
+# Attention over the paged cache: a CTA's first tile of V does not come.  Few rows: requests of 40 tokens, so that
 # in each tile only the threads of the tokens past the length wait for V, and several requests to a CTA; heads of 64 have
 # one barrier more.  Prompts: V's conversion waits.
 @pytest.mark.parametrize("lens,new,Hq,Hkv,dk,dv", [([40] * 256, 1, 4, 4, 128, 128), ([40] * 256, 2, 8, 4, 64, 64),
@@ -122,3 +122,30 @@ def test_attention_without_a_tile_of_v_times_out_and_the_stream_recovers(fp8, le
     out, lse = fp8.fp8_kv_attention(*args, workspace=ws, **kw)
     assert _status(fp8) == 0
     assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_attention_after_a_timeout_writes_nothing_beyond_its_rows(fp8):
+    # The join takes a split request's rows from records that CTAs write with their results.  Here none does, and the
+    # records hold what another call may have left: rows that this call does not have.
+    B, Hq, d, bs, n = 2, 4, 128, 128, 128 * 300
+    kc, ks, vc, vs = fp8.kv_cache(n // bs, 1, bs, d, d)
+    for t in (kc, vc):
+        t.view(torch.uint8).zero_()
+    ks.fill_(1.0)
+    vs.fill_(1.0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    tables = torch.arange(n // bs, **i32).expand(B, -1).contiguous()
+    ws = torch.zeros(8 << 20, dtype=torch.uint8, device="cuda")
+    ws[1 << 14:].view(torch.int64).fill_(B * Hq + 3)
+    big = torch.full((B + 8, Hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B + 8, Hq), 7.0, device="cuda")
+    assert fp8.lib.fp8_debug_set_wait_limit(2_000_000) == 0
+    try:
+        fp8.lib.fp8_debug_skip_one_arrive()
+        fp8.fp8_kv_attention(torch.zeros((B, Hq, d), dtype=torch.bfloat16, device="cuda"), kc, ks, vc, vs, tables,
+                             torch.full((B,), n, **i32), out=big[:B], lse=lse[:B], workspace=ws)
+        assert _status(fp8) == FP8_ERR_TIMEOUT
+    finally:
+        torch.cuda.synchronize()
+        assert fp8.lib.fp8_debug_set_wait_limit(0) == 0
+    assert (big[B:] == 7.0).all() and (lse[B:] == 7.0).all()
