@@ -493,7 +493,8 @@ def fp8_kv_plan(past, new, free_pages, used, tables, block_size, T, lens=None, o
                 positions=None, used_out=None, stream=None):
     """Block tables and slot maps of one step.  past, new int32 [B]; free_pages
     int32 [F], of which used[0] are taken; tables int32 [B, width], completed
-    in place; T token rows.  Returns (lens [B], offsets [B+1], slots [T] int64,
+    in place; T token rows.  No other result may share memory with an input
+    (lens with past, used_out with used).  Returns (lens [B], offsets [B+1], slots [T] int64,
     positions [T] int32, used_out [1])."""
     _cuda(past, "past", _I32, 1)
     _cuda(new, "new", _I32, 1)

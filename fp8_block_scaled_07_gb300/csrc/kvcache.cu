@@ -508,6 +508,16 @@ __global__ void __launch_bounds__(kAppThreads, CTAS) kv_append_kernel(const Appe
     }
 }
 
+// A call's array, for the check that none of its results overlaps another of its arrays.
+struct Span {
+    const void* at;
+    int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return a.at && b.at && a.bytes > 0 && b.bytes > 0 && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+
 bool block_size_ok(int32_t bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
 int log2_of(int32_t bs) {
     int l = 0;
@@ -528,9 +538,15 @@ extern "C" fp8_status fp8_kv_plan(const int32_t* past, const int32_t* fresh, int
     if (static_cast<int64_t>(width) * block_size > (1LL << 31) - 1) return FP8_ERR_INVALID_ARG;
     if (B > kPlanMaxB || T > (1LL << 31) - 1) return FP8_ERR_UNSUPPORTED;
     if (B == 0) return T == 0 ? FP8_OK : FP8_ERR_INVALID_ARG;
-    if (!past || !fresh || !used || !tables || !lens || !offsets || !used_out || used == used_out)
-        return FP8_ERR_INVALID_ARG;
+    if (!past || !fresh || !used || !tables || !lens || !offsets || !used_out) return FP8_ERR_INVALID_ARG;
     if ((n_free > 0 && !free_pages) || (T > 0 && !slots)) return FP8_ERR_INVALID_ARG;
+    // Every CTA reads the inputs while others write results already.
+    const Span arrays[10] = {{tables, 4LL * B * width}, {lens, 4LL * B}, {offsets, 4LL * B + 4}, {slots, 8 * T},
+                             {positions, 4 * T}, {used_out, 4}, {past, 4LL * B}, {fresh, 4LL * B},
+                             {free_pages, 4LL * n_free}, {used, 4}};
+    for (int i = 0; i < 6; ++i)
+        for (int j = i + 1; j < 10; ++j)
+            if (overlap(arrays[i], arrays[j])) return FP8_ERR_INVALID_ARG;
     PlanParams p{};
     p.past = past;
     p.fresh = fresh;

@@ -282,8 +282,10 @@ fp8_status fp8_moe_combine(const void* out, const float* w, const int32_t* pair_
  *   slots [T]         int64, the slot of each token row; -1 for tokens of a
  *                     request that got none and for rows past offsets[B]
  *   positions [T]     (nullable) its position in the request, or -1
- *   used_out [1]      used[0] + pages taken (a buffer other than used)
- * The call only depends on its inputs, so it may be repeated.  B <= 8192,
+ *   used_out [1]      used[0] + pages taken
+ * No result may overlap an input or another result (FP8_ERR_INVALID_ARG), so
+ * lengths are kept in two buffers, not updated in place: the call only
+ * depends on its inputs, and may be repeated.  B <= 8192,
  * width * block_size < 2^31.  slots (and positions) 16-byte aligned are
  * written with wide stores. */
 fp8_status fp8_kv_plan(const int32_t* past, const int32_t* fresh, int32_t B, int32_t block_size,

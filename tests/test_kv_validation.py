@@ -34,6 +34,21 @@ def test_plan(L, want, change):
     assert _call(L.fp8_kv_plan, list(PLAN), PLAN, **change) == want
 
 
+# arrays of their own for B = 4000, T = 9000, two pages free: 1 MB apart
+APART = {k: (i + 1) << 20 for i, k in enumerate(("past", "fresh", "free", "used", "tables", "lens", "offsets", "slots",
+                                                 "positions", "used_out"))}
+
+
+@pytest.mark.parametrize("result,other,shift", [
+    ("lens", "past", 0), ("lens", "fresh", 0), ("lens", "past", 4 * 3999), ("lens", "past", -4 * 3999), ("offsets", "past", 0),
+    ("offsets", "fresh", -16000), ("offsets", "lens", 0), ("tables", "past", 0), ("tables", "free", -48000 + 4),
+    ("slots", "fresh", 0), ("slots", "free", 4), ("positions", "past", 0), ("positions", "slots", 71996),
+    ("used_out", "used", 0), ("used_out", "past", 400), ("used_out", "lens", 0), ("lens", "used", -400)])
+def test_plan_refuses_results_over_other_arrays(L, result, other, shift):
+    base = {**PLAN, **APART, "B": 4000, "T": 9000, "n_free": 2}
+    assert _call(L.fp8_kv_plan, list(PLAN), base, **{result: base[other] + shift}) == INVALID
+
+
 APPEND = dict(k=P, kts=1024, khs=128, v=P, vts=1024, vhs=128, slots=P, T=4, H=8, dk=128, dv=128, kc=P, ks=P, vc=P, vs=P,
               n_pages=7, block=64, fmt=0, stream=None)
 
