@@ -20,7 +20,9 @@
 //     2^-13 of the row's largest element hi is subnormal and the rest is kept
 //     to 2^-22 of that element.)
 //   * few rows: a probability p in fp32 becomes hi + lo / 32 the same way: 9
-//     significant bits, one more than bf16's.  Many rows: p is rounded to
+//     significant bits, one more than bf16's, down to 2^-9 of the row's
+//     largest p; below that a multiple of 2^-18 of it, rounded so that the
+//     errors of many cancel (attention_few.cu).  Many rows: p is rounded to
 //     fp16, 11 significant bits.
 // Few rows: one MMA serves both halves, which are separate columns of its N
 // side.  Many rows: two MMAs add to one accumulator.
@@ -194,16 +196,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
         : "memory");
 }
 
-// Two values as e4m3 pairs hi and lo with value = hi + lo / 32 (kScaled) or
-// hi + lo: through fp16, whose 11 significant bits hold the difference exactly.
-template <bool kScaled>
-__device__ __forceinline__ void split_e4m3x2(float a, float b, uint16_t& hi, uint16_t& lo) {
+// Two values as e4m3 pairs hi and lo with value = hi + lo / 32: through fp16,
+// whose 11 significant bits hold the difference exactly.  `dither` (two fp16)
+// is added to lo before it is rounded.
+__device__ __forceinline__ void split_e4m3x2(float a, float b, uint16_t& hi, uint16_t& lo, uint32_t dither = 0) {
     uint32_t p2, h2;
     hi = f32x2_to_e4m3x2(a, b);   // (from fp16 it takes twice the issue slots)
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p2) : "f"(b), "f"(a));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(hi));
     asm("sub.f16x2 %0, %1, %2;" : "=r"(p2) : "r"(p2), "r"(h2));
-    if (kScaled) asm("mul.f16x2 %0, %1, %2;" : "=r"(p2) : "r"(p2), "r"(0x50005000u));   // 32, 32
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p2) : "r"(p2), "r"(0x50005000u), "r"(dither));   // 32, 32
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(p2));
 }
 

@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
                     unpack_bf16x8(v[k], f);
                     uint16_t hi[4], lo[4];
 #pragma unroll
-                    for (int i2 = 0; i2 < 4; ++i2) split_e4m3x2<true>(f[2 * i2] * up, f[2 * i2 + 1] * up, hi[i2], lo[i2]);
+                    for (int i2 = 0; i2 < 4; ++i2) split_e4m3x2(f[2 * i2] * up, f[2 * i2 + 1] * up, hi[i2], lo[i2]);
                     if (sub < kRows && r < RU) {
                         const uint2 ph = make_uint2(hi[0] | (static_cast<uint32_t>(hi[1]) << 16), hi[2] | (static_cast<uint32_t>(hi[3]) << 16));
                         const uint2 pl = make_uint2(lo[0] | (static_cast<uint32_t>(lo[1]) << 16), lo[2] | (static_cast<uint32_t>(lo[3]) << 16));
@@ -754,6 +754,12 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
 #pragma unroll
                 for (int r = 0; r < RU; ++r) y[r] = -INFINITY;
             }
+            // The last place of hi + lo / 32 is 2^-14, and thousands of probabilities below half of that, next to a
+            // large one, would all become 0 (or, a little above, be rounded the same way).  So what lo is rounded
+            // from is shifted by up to half a place either way, by the golden ratio's multiples modulo 1, which lie
+            // evenly in any run of tokens: the errors of like probabilities cancel.  (A 0 stays 0.)
+            uint32_t dither;   // ten bits of the multiple m in [0, 1) as (1 + m) 2^-9, less 1.5 * 2^-9
+            asm("sub.f16x2 %0, %1, %2;" : "=r"(dither) : "r"(((static_cast<uint32_t>(tok) * 0x9E3779B9u) >> 22) * 0x10001u + 0x18001800u), "r"(0x1A001A00u));
             // The maxima stay while every probability fits: then one barrier,
             // which also says so, is all that the warps share of a tile.  Not
             // before every row has a maximum, though: one that has seen nothing
@@ -815,6 +821,8 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
             }
             if (i >= 2) ok = mbar_wait(&pvdone[buf], ((i - 2) >> 1) & 1, abort_flag) && ok;   // P is free
             uint8_t* P = sP + buf * F::kPBytes + (F::kPair == 2 ? (t & 1) * N * 128 : 0);
+            int kx = kb;   // (new for the compiler at each tile: the rows' eight addresses, kept through the loop, spill)
+            asm volatile("" : "+r"(kx));
             // P, split, in the layout the MMA reads: row n of 128 bytes, byte = token (or pair)
 #pragma unroll
             for (int r = 0; r < RU; r += 2) {
@@ -823,13 +831,13 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
                 const float p0 = ex2(y[r]);
                 const float p1 = two ? ex2(y[r1]) : 0.0f;
                 uint16_t hi, lo;
-                split_e4m3x2<true>(p0, p1, hi, lo);
-                const int a0 = r * 128 + (((kb >> 4) ^ (r & 7)) << 4) + (kb & 15);
+                split_e4m3x2(p0, p1, hi, lo, dither);
+                const int a0 = r * 128 + (kx ^ ((r & 7) << 4));
                 l[r] = fmaf(p0, iv, l[r]);
                 P[a0] = static_cast<uint8_t>(hi);
                 P[NR * 128 + a0] = static_cast<uint8_t>(lo);
                 if (two) {
-                    const int a1 = r1 * 128 + (((kb >> 4) ^ (r1 & 7)) << 4) + (kb & 15);
+                    const int a1 = r1 * 128 + (kx ^ ((r1 & 7) << 4));
                     l[r1] = fmaf(p1, iv, l[r1]);
                     P[a1] = static_cast<uint8_t>(hi >> 8);
                     P[NR * 128 + a1] = static_cast<uint8_t>(lo >> 8);

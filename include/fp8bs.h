@@ -322,6 +322,9 @@ fp8_status fp8_kv_append(const void* k, int64_t k_token_stride, int64_t k_head_s
  * out is 32-byte aligned.  (dk, dv) in {(64, 64), (128, 128), (192, 128)},
  * else FP8_ERR_UNSUPPORTED.  Sums and softmax statistics are fp32; the
  * probabilities enter the second product with 9 significant bits or more.
+ * (With few rows per request, one below 2^-9 of its row's largest is a
+ * multiple of 2^-18 of that, rounded up or down by the token's position, so
+ * that the errors of many like ones cancel.)
  * workspace: device buffer of at least
  * fp8_kv_attention_workspace_size bytes, under fp8_gemm's rule: zero-filled
  * before its first use, and left ready for the next call by every call that

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import oracle
+import synthetic as syn
 from oracle import kv
 from tests.helpers import host_bits
 from tests.test_gpu_kv_attention import _case, _check, _run
@@ -52,3 +53,45 @@ def test_ranges_that_begin_in_a_hole(fp8, lens, Hkv, G, dk, dv):
     for b in range(len(lens)):
         c["tables"][b, b:-(-lens[b] // 128):3] = -1
     _check(fp8, c, ragged=False)
+
+
+# ------------------------------------------------------------------ many small probabilities
+# One token with weight 1 and thousands with e^-gap each, V with a common
+# mean: together the small ones count.  They enter the product in multiples of
+# 2^-18 of the largest, rounded either way: an error of at most that each, and
+# at most half of it in the mean square, so that six standard deviations of
+# the sum are 6 * 2^-19 * sqrt(sum v^2) (over sum p).  The rest of the bound:
+# bf16's result, 9 significant bits of a probability, the scores' 2^-16.
+@pytest.mark.parametrize("Hq,Hkv,dk,dv", [(8, 8, 64, 64), (32, 8, 128, 128), (16, 1, 128, 128)])
+@pytest.mark.parametrize("flat", [True, False])
+def test_many_small_probabilities(fp8, Hq, Hkv, dk, dv, flat):
+    B, n, bs = 320 // Hkv, 8192, 128     # requests over the same pages: a range holds whole segments
+    rng = np.random.default_rng(dk + Hq)
+    P = n // bs
+    kc = np.zeros((P, Hkv, bs, dk), np.uint8)
+    if not flat:   # scores of a standard deviation of some 0.3
+        kc[:] = oracle.e4m3_encode(rng.standard_normal(kc.shape).astype(np.float32) * 0.25).reshape(kc.shape)
+    kc[0, :, 0] = oracle.e4m3_encode(np.ones(dk, np.float32))
+    vc = oracle.e4m3_encode((1 + 0.25 * rng.standard_normal((P, Hkv, bs, dv))).astype(np.float32)).reshape(P, Hkv, bs, dv)
+    one = np.ones((P, Hkv), np.float32)
+    gaps = rng.choice([9.0, 11.0, 13.0, 13.5, 14.0], (B, Hq, 1))
+    noise = rng.standard_normal((B, Hq, dk)) * (0.0 if flat else 0.3)
+    q = syn.to_bf16_bits((gaps / np.sqrt(dk) + noise).astype(np.float32))
+    c = dict(q=q, kc=kc, ks=one, vc=vc, vs=one, tables=np.tile(np.arange(P, dtype=np.int32), (B, 1)),
+             lens=np.full(B, n, np.int32), offsets=np.arange(B + 1, dtype=np.int32), sm=dk ** -0.5)
+    out, lse = _run(fp8, c, ragged=False)
+    got = oracle.bf16_to_f32(host_bits(out)).astype(np.float64).reshape(B, Hq, dv)
+    some = [0, B // 3, B - 1]
+    kf, vf = (oracle.e4m3_decode(x).astype(np.float64).reshape(P, Hkv, bs, -1).transpose(1, 0, 2, 3).reshape(Hkv, n, -1)
+              for x in (kc, vc))
+    qf = oracle.bf16_to_f32(q).astype(np.float64).reshape(B, Hq, dk)
+    for b in some:
+        for h in range(Hq):
+            k, v = kf[h * Hkv // Hq], vf[h * Hkv // Hq]
+            s = k @ qf[b, h] * c["sm"]
+            p = np.exp(s - s.max())
+            want = p @ v / p.sum()
+            tol = (np.abs(want) * 2.0 ** -8 + p @ np.abs(v) / p.sum() * (2.0 ** -9 + 2.0 ** -16) +
+                   6 * 2.0 ** -19 * np.sqrt((v * v).sum(0)) / p.sum())
+            assert (np.abs(got[b, h] - want) <= tol).all(), (b, h, np.abs(got[b, h] - want).max(), tol.max())
+            assert abs(float(lse[b, h]) - (s.max() + np.log(p.sum()))) <= 2.0 ** -13
