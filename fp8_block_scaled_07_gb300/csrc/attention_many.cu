@@ -52,6 +52,8 @@ constexpr int kRegsLow = 96, kRegsHigh = 160, kRegsLaunch = 128;
 static_assert(2 * kRegsLow + 2 * kRegsHigh == 4 * kRegsLaunch, "what some give, others take");
 constexpr int kItems = 4;           // items announced ahead
 constexpr float kPBits = 8.0f, kSlack = 7.0f;   // 2^15 < 65504
+constexpr uint32_t kOdd = 1u << 31;             // of a tile: some page's scale of K is not at least kLeast
+constexpr float kLeast = 0x1p-60f;              // (two factors of so much have a product above 0)
 
 template <int DK, int DV>
 struct Many {
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* s_len = reinterpret_cast<int*>(s_page + kRing * 8);
     int* s_n = s_len + kManyB;
     int* s_first = s_n + kManyB;
-    uint32_t* s_dead = reinterpret_cast<uint32_t*>(s_first + kManyB);       // [kRing] pages that are left out, as bits
+    uint32_t* s_dead = reinterpret_cast<uint32_t*>(s_first + kManyB);       // [kRing] pages that are left out, as bits; kOdd
     float* s_qf = reinterpret_cast<float*>(s_dead + kRing);                 // [256] factor of a row's S
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_qf + 256);
     uint64_t* kfull = bars;
@@ -518,7 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 const bool on = vs > 0.0f;
                 const bool there = lane < pages_per_tile && i * 128 + lane * bs < m.len;
-                const uint32_t dead = __ballot_sync(0xFFFFFFFFu, there && !on);
+                uint32_t dead = __ballot_sync(0xFFFFFFFFu, there && !on);
+                if (__any_sync(0xFFFFFFFFu, there && on && !(ks >= kLeast))) dead |= kOdd;
                 if (lane < 8) s_page[slot * 8 + lane] = on ? make_float4(ks, log2f(vs), 1.0f / vs, 0.0f) : make_float4(1.0f, 0.0f, 0.0f, 0.0f);
                 if (lane == 0) s_dead[slot] = dead;
                 __syncwarp();
@@ -749,10 +752,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&iempty[k % kItems]);
             float qf = 1.0f;
+            bool odd_rows = false;   // (of the warp's)
             if (steps > 0) {
                 ok = mbar_wait(&qfull[tile], nq & 1, abort_flag) && ok;
                 ++nq;
                 qf = s_qf[tile * 128 + t];
+                odd_rows = __any_sync(0xFFFFFFFFu, row >= 0 && !(qf >= kLeast)) != 0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&qread[tile]);
             }
@@ -785,6 +790,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32(tS + hv * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
                     tmem_wait_ld();
                     if (masked) {
+                        // A factor that is zero (K's scale may be, or the product) would make NaN of an -inf, and
+                        // a negative one turns round the order that the maximum below goes by: then x itself.
+                        if (odd_rows || (dead & kOdd) != 0) {
+#pragma unroll
+                            for (int k2 = 0; k2 < 64; ++k2)
+                                r[k2] = __float_as_uint(fmaf(__uint_as_float(r[k2]), ck[k2 / 16], lv[k2 / 16]));
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                ck[q] = 1.0f;
+                                lv[q] = 0.0f;
+                            }
+                        }
                         const int left = lim - i * 128 - col0;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {

@@ -95,3 +95,20 @@ def test_many_small_probabilities(fp8, Hq, Hkv, dk, dv, flat):
                    6 * 2.0 ** -19 * np.sqrt((v * v).sum(0)) / p.sum())
             assert (np.abs(got[b, h] - want) <= tol).all(), (b, h, np.abs(got[b, h] - want).max(), tol.max())
             assert abs(float(lse[b, h]) - (s.max() + np.log(p.sum()))) <= 2.0 ** -13
+
+
+# ------------------------------------------------------------------ K's scale is zero, negative or lost in a product
+@pytest.mark.parametrize("Hq,Hkv,dk,dv", [(8, 2, 128, 128), (4, 4, 64, 64), (3, 3, 192, 128)])
+@pytest.mark.parametrize("new", [[1, 1], [2, 3], [200, 70]])
+@pytest.mark.parametrize("scale,q_std", [(0.0, 1.0), (-0.0, 1.0), (-0.01, 30.0)])
+def test_scales_of_k_that_are_not_positive(fp8, Hq, Hkv, dk, dv, new, scale, q_std):
+    c = _case([400, 300], new, 32, Hq, Hkv, dk, dv, seed=17, q_std=q_std)
+    for b, i in ((0, 1), (0, 7), (0, 12), (1, 0), (1, 8)):   # in tiles that every row sees, and in the last
+        c["ks"][c["tables"][b, i]] = np.float32(scale)
+    _check(fp8, c, ragged=new[0] > 1)
+
+
+def test_products_of_scales_that_underflow(fp8):
+    for new in ([1, 1], [200, 70]):
+        c = _case([400, 300], new, 32, 8, 2, 128, 128, seed=18, q_std=0.0, sm_scale=1e-20)
+        _check(fp8, c, ragged=new[0] > 1)
