@@ -166,6 +166,45 @@ __device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
     return d;
 }
 
+// Whether any of 16 e4m3 codes is a NaN (0x7F, 0xFF): not 0.
+__device__ __forceinline__ uint32_t e4m3_nans(const uint4& v) {
+    constexpr uint32_t kAbs = 0x7F7F7F7Fu, kOne = 0x01010101u;
+    return (((v.x & kAbs) + kOne) | ((v.y & kAbs) + kOne) | ((v.z & kAbs) + kOne) | ((v.w & kAbs) + kOne)) & 0x80808080u;
+}
+
+// V of a token that only some rows see must not hold a NaN: 0 x NaN would enter
+// the sums of the others.  Such a NaN becomes 0, and where it stood is noted:
+// key[d], for each value d, is the first token with one, as an offset from a
+// token that the rows have in common, above a tag that says whose note it is
+// (a later one's passes over an earlier one's, so notes are never cleared).
+// The results of the rows that see that token are made NaN in the end.
+template <int kBits>
+__device__ __forceinline__ uint32_t nan_key(uint32_t tag, int offset) {
+    return (tag << kBits) | ((1u << kBits) - 1u - static_cast<uint32_t>(offset));
+}
+// Notes the NaNs among 16 codes of values d .. d + 15 (key: d's).
+__device__ __forceinline__ void note_nans(const uint4& v, uint32_t* key, uint32_t mine) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b)
+            if (((w[i] >> (8 * b)) & 0x7Fu) == 0x7Fu) atomicMax(key + 4 * i + b, mine);
+}
+// 16 codes, 0 for every NaN.
+__device__ __forceinline__ uint4 without_nans(uint4 v) {
+    auto of = [](uint32_t x) {
+        const uint32_t n = ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+        return x & ~(n | (n - (n >> 7)));
+    };
+    return make_uint4(of(v.x), of(v.y), of(v.z), of(v.w));
+}
+// Whether a row that sees the tokens below `limit` (as an offset) sees the noted one.
+template <int kBits>
+__device__ __forceinline__ bool sees_nan(uint32_t key, uint32_t tag, int limit) {
+    return (key >> kBits) == tag && limit > static_cast<int>((1u << kBits) - 1u - (key & ((1u << kBits) - 1u)));
+}
+
 // N consecutive TMEM columns of this thread's lane, as fp32.
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {

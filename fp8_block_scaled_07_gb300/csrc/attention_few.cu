@@ -29,6 +29,8 @@
 // stage is free after S, V's only after O, and V gets twice the stages.
 #include "attention.cuh"
 
+#include <type_traits>
+
 namespace fp8bs {
 namespace {
 
@@ -37,6 +39,7 @@ constexpr float kMostBits = 8.0f;   // and at most 256 with one that has since b
                                     // hi that lo has to hold is 256 there, below e4m3's 448
 constexpr int kThreads = 256;
 constexpr int kJoinThreads = 256;
+constexpr int kNanBits = 8;         // a request of this kernel has at most 128 rows, and so few tokens that only some see
 
 // A part: O of each row, then (M, l) of each; a multiple of 16 bytes.
 __host__ __device__ constexpr int part_floats(int ru, int dv) { return ru * dv + (ru < 2 ? 4 : 2 * ru); }
@@ -46,8 +49,9 @@ __host__ __device__ constexpr int info_ints(int ru) { return 4 + (ru < 2 ? 4 : 2
 // CTAs per SM: rows cost registers.
 __host__ __device__ constexpr int few_blocks(int ru) { return ru > 16 ? 1 : 2; }
 
-// RU: the rows that are computed; the MMA has at least NR = 8.
-template <int DK, int DV, int RU>
+// RU: the rows that are computed; the MMA has at least NR = 8.  kSeveral: a
+// request may have several queries, and then tokens that only some rows see.
+template <int DK, int DV, int RU, bool kSeveral>
 struct Few {
     static constexpr int NR = RU < 8 ? 8 : RU;
     static constexpr bool kWide = DK >= 128;                  // a 128-byte slab of K ...
@@ -60,13 +64,14 @@ struct Few {
     static constexpr int kCols = 2 * kN + 2 * kON;
     static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static constexpr int kBlocks = few_blocks(RU);
+    static constexpr int kBars = 448;
     static constexpr int kPairX = DV == 64 ? RU * 64 : 0;     // the odd tokens' half of O (floats)
-    static constexpr int kMisc = 2 * NR * 8 + (3 * kFewB + 12) * 4 + (4 * RU + 8 * RU + 2 * RU + 2 * NR + 2 * NR + 16) * 4 +
-                                 kRing * 8 * 12 + kPairX * 4 + 512;
+    static constexpr int kMisc = 2 * NR * 8 + (3 * kFewB + 12) * 4 + (4 * RU + 8 * RU + 2 * RU + 2 * NR + 2 * NR) * 4 +
+                                 kRing * 8 * 12 + kPairX * 4 + (kSeveral ? (2 * DV + 2) * 4 : 0) + 8 + kBars;
     static constexpr int kFixed = 1024 + 2 * kQBytes + 2 * kPBytes + kMisc;
-    static constexpr int kBudget = (kBlocks == 1 ? 227 : 113) * 1024 - 128;
+    static constexpr int kBudget = (kBlocks == 1 ? 227 : 113) * 1024 - 64;   // (64: s_scan)
     // K's stages are a third of the space (2 at least), V's the rest
-    static constexpr int kSK = (kBudget - kFixed) / 3 / kKBytes < 2 ? 2 : (kBudget - kFixed) / 3 / kKBytes > 4 ? 4 : (kBudget - kFixed) / 3 / kKBytes;
+    static constexpr int kSK = (kBudget - kFixed + 1024) / 3 / kKBytes < 2 ? 2 : (kBudget - kFixed + 1024) / 3 / kKBytes > 4 ? 4 : (kBudget - kFixed + 1024) / 3 / kKBytes;
     static constexpr int kFitV = (kBudget - kFixed - kSK * kKBytes) / kVBytes;
     static constexpr int kSV = kFitV > 8 ? 8 : kFitV;
     static constexpr int kSmem = kFixed + kSK * kKBytes + kSV * kVBytes;
@@ -151,11 +156,11 @@ struct Patience {
     }
 };
 
-template <int DK, int DV, int RU>
-__global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
+template <int DK, int DV, int RU, bool kSeveral>
+__global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU, kSeveral>::kBlocks))
     attn_few_kernel(const __grid_constant__ CUtensorMap tm_k0, const __grid_constant__ CUtensorMap tm_k1,
                     const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
-    using F = Few<DK, DV, RU>;
+    using F = Few<DK, DV, RU, kSeveral>;
     using Walk = TileWalk<F::kSegment>;
     constexpr int kSegment = F::kSegment;
     constexpr int SK = F::kSK, SV = F::kSV, NR = F::NR, N = F::kN, ON = F::kON;
@@ -179,7 +184,9 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
     float* s_lv = s_ck + kRing * 8;                  // log2(v_scale), -inf: the page is left out
     float* s_iv = s_lv + kRing * 8;                  // 1 / v_scale, or 0
     float* s_x = s_iv + kRing * 8;                   // dv = 64: [RU][64]
-    uint64_t* bars = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(s_x + F::kPairX) + 7) & ~static_cast<uintptr_t>(7));
+    uint32_t* s_nan = reinterpret_cast<uint32_t*>(s_x + F::kPairX);          // [2 segments][DV] NaNs in V (nan_key)
+    uint32_t* s_nans = s_nan + 2 * DV;               // [2] the last segment that has one
+    uint64_t* bars = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(s_nan + (kSeveral ? 2 * DV + 2 : 0)) + 7) & ~static_cast<uintptr_t>(7));
     uint64_t* kfull = bars;
     uint64_t* kempty = kfull + SK;
     uint64_t* vfull = kempty + SK;
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     __shared__ int2 s_scan[kThreads / 32];
-    static_assert((2 * SK + 2 * SV + 8 + 2 * kRing + 4 + 1) * 8 + 16 + 8 <= 512, "barrier block");
+    static_assert((2 * SK + 2 * SV + 8 + 2 * kRing + 4 + 1) * 8 + 16 + 8 <= F::kBars, "barrier block");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -231,6 +238,8 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
         tmem_alloc(tmem_holder, F::kTmem);
         tmem_relinquish();
     }
+    if constexpr (kSeveral)
+        for (int i = threadIdx.x; i < 2 * DV + 2; i += kThreads) s_nan[i] = 0;
     if constexpr (RU < NR) {   // rows that are only there for the MMA stay zero
         uint4* z = reinterpret_cast<uint4*>(sQ);
         for (int i = threadIdx.x; i < (2 * F::kQBytes + 2 * F::kPBytes) / 16; i += kThreads) z[i] = make_uint4(0, 0, 0, 0);
@@ -668,6 +677,15 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
             }
             const bool writes = F::kPair == 1 || w4 < 2;
             const int d = t;
+            if constexpr (kSeveral) {
+                if (s_nans[par] == static_cast<uint32_t>(done.sg + 1) && writes) {   // (rare)
+                    const uint32_t key = s_nan[par * DV + d];
+#pragma unroll
+                    for (int r = 0; r < RU; ++r)
+                        if (sees_nan<kNanBits>(key, done.sg + 1, s_lim[par * NR + r] - s_min[par]))
+                            o[r] = __uint_as_float(0x7FC00000u);
+                }
+            }
             // lane r knows row r: its sum, its place
             const float* sl = s_l + par * 4 * RU;
             const int mr = lane % RU;
@@ -843,15 +861,27 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU>::kBlocks))
                     P[NR * 128 + a1] = static_cast<uint8_t>(lo >> 8);
                 }
             }
-            // V of a token that is not there may hold anything, a NaN too: zero it
-            if (tok >= len || lv == -INFINITY) {
+            // V of a token that is not there may hold anything, a NaN too: zero it.  One that only some rows see
+            // keeps its numbers (note_nans).
+            if (tok >= (kSeveral ? least : len) || lv == -INFINITY) {
                 const int st = i % SV;
                 ok = mbar_wait(&vfull[st], (i / SV) & 1, abort_flag) && ok;
                 uint8_t* vr = sV + st * F::kVBytes + kb * 128;
+                auto chunk = [&](int c) {
+                    return reinterpret_cast<uint4*>(vr + (((c + (F::kPair == 2 ? (t & 1) * 4 : 0)) ^ (kb & 7)) << 4));
+                };
+                if (!kSeveral || tok >= len || lv == -INFINITY) {
 #pragma unroll
-                for (int c = 0; c < DV / 16; ++c) {
-                    const int chunk = c + (F::kPair == 2 ? (t & 1) * 4 : 0);
-                    *reinterpret_cast<uint4*>(vr + ((chunk ^ (kb & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < DV / 16; ++c) *chunk(c) = make_uint4(0, 0, 0, 0);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < DV / 16; ++c) {
+                        const uint4 v = *chunk(c);
+                        if (e4m3_nans(v) == 0) continue;
+                        *chunk(c) = without_nans(v);
+                        note_nans(v, s_nan + (sg & 1) * DV + c * 16, nan_key<kNanBits>(sg + 1, tok - least));
+                        s_nans[sg & 1] = sg + 1;
+                    }
                 }
             }
             fence_proxy_async_smem();
@@ -991,19 +1021,19 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
     if (p.lse && lane == 0) p.lse[at] = l == 0.0f ? -INFINITY : (m - kPBits + log2f(l)) * kLn2;
 }
 
-template <int DK, int DV, int RU>
+template <int DK, int DV, int RU, bool kSeveral>
 cudaError_t launch(const AttnMaps& m, const AttnParams& p, int sms, cudaStream_t st) {
-    using F = Few<DK, DV, RU>;
+    using F = Few<DK, DV, RU, kSeveral>;
     static int configured[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !configured[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_few_kernel<DK, DV, RU>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
+        const cudaError_t e = cudaFuncSetAttribute(attn_few_kernel<DK, DV, RU, kSeveral>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
         if (e != cudaSuccess) return e;
         if (dev < 64) configured[dev] = 1;
     }
     const int ctas = sms * F::kBlocks;
-    const cudaError_t e = launch_pdl(attn_few_kernel<DK, DV, RU>, dim3(ctas), dim3(kThreads), F::kSmem, st, m.k0, m.k1, m.v, p);
+    const cudaError_t e = launch_pdl(attn_few_kernel<DK, DV, RU, kSeveral>, dim3(ctas), dim3(kThreads), F::kSmem, st, m.k0, m.k1, m.v, p);
     if (e != cudaSuccess) return e;
     // at most so many ranges: those of the longest lengths the tables can hold
     const int64_t positions = static_cast<int64_t>(p.B) * ((static_cast<int64_t>(p.width) << p.bs_log2) / 128 + 1 + F::kSegment) * p.Hkv *
@@ -1013,15 +1043,15 @@ cudaError_t launch(const AttnMaps& m, const AttnParams& p, int sms, cudaStream_t
     return launch_pdl(attn_join_kernel<DV, RU>, dim3(static_cast<unsigned>(ranges - 1), RU < 8 ? 1 : RU / 8), dim3(kJoinThreads), 0, st, p);
 }
 
-template <int DK, int DV>
+template <int DK, int DV, bool kSeveral>
 cudaError_t launch_rows(int ru, const AttnMaps& m, const AttnParams& p, int sms, cudaStream_t st) {
     switch (ru) {
-        case 1: return launch<DK, DV, 1>(m, p, sms, st);
-        case 4: return launch<DK, DV, 4>(m, p, sms, st);
-        case 8: return launch<DK, DV, 8>(m, p, sms, st);
-        case 16: return launch<DK, DV, 16>(m, p, sms, st);
+        case 1: return launch<DK, DV, 1, kSeveral>(m, p, sms, st);
+        case 4: return launch<DK, DV, 4, kSeveral>(m, p, sms, st);
+        case 8: return launch<DK, DV, 8, kSeveral>(m, p, sms, st);
+        case 16: return launch<DK, DV, 16, kSeveral>(m, p, sms, st);
     }
-    return launch<DK, DV, 32>(m, p, sms, st);
+    return launch<DK, DV, 32, kSeveral>(m, p, sms, st);
 }
 
 size_t info_bytes(int ru, int sms) { return (4 + static_cast<size_t>(sms) * few_blocks(ru) * info_ints(ru)) * sizeof(int32_t); }
@@ -1045,9 +1075,13 @@ void few_workspace_split(AttnParams& p, void* base, int ru, int sms) {
 }
 
 cudaError_t launch_few(int dk, int ru, const AttnMaps& m, const AttnParams& p, int sms, cudaStream_t st) {
-    return dk == 64    ? launch_rows<64, 64>(ru, m, p, sms, st)
-           : dk == 128 ? launch_rows<128, 128>(ru, m, p, sms, st)
-                       : launch_rows<192, 128>(ru, m, p, sms, st);
+    auto of = [&](auto several) {
+        constexpr bool S = decltype(several)::value;
+        return dk == 64    ? launch_rows<64, 64, S>(ru, m, p, sms, st)
+               : dk == 128 ? launch_rows<128, 128, S>(ru, m, p, sms, st)
+                           : launch_rows<192, 128, S>(ru, m, p, sms, st);
+    };
+    return p.offsets ? of(std::true_type()) : of(std::false_type());
 }
 int few_read_and_clear_status(cudaStream_t st) { return read_and_clear_attention_status(st); }
 bool few_set_wait_limit(long long cycles) { return set_attention_wait_limit(cycles); }

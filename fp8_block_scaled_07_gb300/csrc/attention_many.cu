@@ -51,6 +51,9 @@ constexpr int kThreads = 512;
 constexpr int kRegsLow = 96, kRegsHigh = 160, kRegsLaunch = 128;
 static_assert(2 * kRegsLow + 2 * kRegsHigh == 4 * kRegsLaunch, "what some give, others take");
 constexpr int kItems = 4;           // items announced ahead
+constexpr int kNotes = 8;           // items whose notes of NaNs in V are kept: the last one's are read once the next has begun
+static_assert(kNotes > kItems + 1, "the results of an item are written before the item kItems + 1 on is announced");
+constexpr int kNanBits = 9;         // tokens of an item that only some rows see, and those to the end of their tile: 383 at most
 constexpr float kPBits = 8.0f, kSlack = 7.0f;   // 2^15 < 65504
 constexpr uint32_t kOdd = 1u << 31;             // of a tile: some page's scale of K is not at least kLeast
 constexpr float kLeast = 0x1p-60f;              // (two factors of so much have a product above 0)
@@ -63,7 +66,7 @@ struct Many {
     static constexpr int kSK = DK == 192 ? 2 : 3;              // stages of K, of V's codes, of V in fp16
     static constexpr int kSV = 2;
     static constexpr int kSF = DK == 192 ? 1 : 2;
-    static constexpr int kMisc = kManyB * 20 + 16 + kRing * 8 * 16 + kRing * 4 + 256 * 4 + kItems * 48 + 1024;
+    static constexpr int kMisc = kManyB * 20 + 16 + kRing * 8 * 16 + kRing * 4 + 256 * 4 + kItems * 48 + kNotes * (DV + 2) * 4 + 1024;
     static constexpr int kSmem = 1024 + 4 * kQTile + kSK * kKBytes + kSV * kVBytes + kSF * kFBytes + kMisc;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -195,7 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* s_first = s_n + kManyB;
     uint32_t* s_dead = reinterpret_cast<uint32_t*>(s_first + kManyB);       // [kRing] pages that are left out, as bits; kOdd
     float* s_qf = reinterpret_cast<float*>(s_dead + kRing);                 // [256] factor of a row's S
-    uint64_t* bars = reinterpret_cast<uint64_t*>(s_qf + 256);
+    uint32_t* s_nan = reinterpret_cast<uint32_t*>(s_qf + 256);              // [kNotes][DV] NaNs in V (nan_key), as offsets from
+    int* s_base = reinterpret_cast<int*>(s_nan + kNotes * DV);              // [kNotes] the tokens that all of the item's rows see
+    uint32_t* s_nans = reinterpret_cast<uint32_t*>(s_base + kNotes);        // [kNotes] the last item with such a NaN, plus 1
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s_nans + kNotes);
     uint64_t* kfull = bars;
     uint64_t* kempty = kfull + SK;
     uint64_t* vfull = kempty + SK;
@@ -218,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert((2 * SK + 2 * SV + 4 * SF + 16 + 2 * kRing + 2 * kItems + 1) * 8 + 8 <= 1024, "barrier block");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < kNotes * (DV + 2); i += kThreads) s_nan[i] = 0;
     if (threadIdx.x == 0) {
         for (int i = 0; i < SK; ++i) {
             mbar_init(&kfull[i], 1);
@@ -511,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 a = on ? __ldg(p.k_scale + at) : 0.0f;
                 b = on ? __ldg(p.v_scale + at) : 0.0f;
             };
+            const int all_see = limit(m, m.row0), note = k % kNotes;
             if (m.nmax > 0) scales_of(page_of(m, 0), ks, vs);
             if (m.nmax > 1) scales_of(page_of(m, 1), ks1, vs1);
             int page2 = m.nmax > 2 ? page_of(m, 2) : -1;
@@ -522,6 +530,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool there = lane < pages_per_tile && i * 128 + lane * bs < m.len;
                 uint32_t dead = __ballot_sync(0xFFFFFFFFu, there && !on);
                 if (__any_sync(0xFFFFFFFFu, there && on && !(ks >= kLeast))) dead |= kOdd;
+                if (i * 128 + 128 > all_see) {
+                    // NaNs in V of tokens that only some of the item's rows see: taken out and noted (note_nans) before
+                    // the conversion, which waits for these constants.  Here, in the codes, they cost 0 to 2% of a
+                    // prompt's time; looked for by the warps that convert, 3 to 7%.
+                    // (The stage's tile before it must be done with first: a phase is told from the next, not from the
+                    // one after that.)
+                    const int st = g % SV, was = g - SV;
+                    ok = was < 0 || mbar_wait(&cempty[was % kRing], (was / kRing) & 1, abort_flag);
+                    ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(&vfull[st], (g / SV) & 1, abort_flag)) != 0;
+                    if (!ok) break;
+                    uint8_t* v = sV + st * F::kVBytes;
+                    constexpr int kCh = DV / 16;   // 16 codes each
+#pragma unroll 1
+                    for (int x0 = lane; x0 < 128 * kCh; x0 += 128) {
+                        uint32_t nans = 0;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) nans |= e4m3_nans(*reinterpret_cast<const uint4*>(v + (x0 + u * 32) * 16));
+                        if (nans == 0) continue;
+#pragma unroll 1
+                        for (int x = x0; x < x0 + 128; x += 32) {
+                            const int r = x / kCh, c = (x % kCh) ^ (DV == 128 ? r & 7 : (r >> 1) & 3), tok = i * 128 + r;
+                            uint4* at = reinterpret_cast<uint4*>(v + x * 16);
+                            const uint4 codes = *at;
+                            if (tok < all_see || tok >= m.len || ((dead >> (r >> p.bs_log2)) & 1) || e4m3_nans(codes) == 0) continue;
+                            *at = without_nans(codes);
+                            note_nans(codes, s_nan + note * DV + c * 16, nan_key<kNanBits>(k + 1, tok - all_see));
+                            s_base[note] = all_see;
+                            s_nans[note] = k + 1;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
                 if (lane < 8) s_page[slot * 8 + lane] = on ? make_float4(ks, log2f(vs), 1.0f / vs, 0.0f) : make_float4(1.0f, 0.0f, 0.0f, 0.0f);
                 if (lane == 0) s_dead[slot] = dead;
                 __syncwarp();
@@ -732,6 +772,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     tc_fence_before();
+                    const uint32_t last = k - 1, note = last % kNotes;
+                    if (s_nans[note] == last + 1 && row >= 0) {   // (rare)
+#pragma unroll 1
+                        for (int d = 0; d < DV; ++d)
+                            if (sees_nan<kNanBits>(s_nan[note * DV + d], last + 1, lim - s_base[note]))
+                                p.out[row * DV + d] = __float2bfloat16_rn(__uint_as_float(0x7FC00000u));
+                    }
                 } else if (row >= 0) {
 #pragma unroll
                     for (int k2 = 0; k2 < DV / 8; ++k2) dst[k2] = make_uint4(0, 0, 0, 0);

@@ -112,3 +112,38 @@ def test_products_of_scales_that_underflow(fp8):
     for new in ([1, 1], [200, 70]):
         c = _case([400, 300], new, 32, 8, 2, 128, 128, seed=18, q_std=0.0, sm_scale=1e-20)
         _check(fp8, c, ragged=new[0] > 1)
+
+
+# ------------------------------------------------------------------ NaN in V
+def _check_rows(fp8, c, T=None):
+    """Every row against the oracle's answer for it alone, with the tokens that it sees and no others."""
+    out, lse = _run(fp8, c)
+    new = np.diff(c["offsets"])
+    T = int(c["offsets"][-1])
+    req = np.repeat(np.arange(len(new)), new)
+    j = np.arange(T) - c["offsets"][req]
+    lims = np.maximum(0, c["lens"][req] - new[req] + j + 1).astype(np.int32)
+    want, wl, tol, eps = kv.attention(c["q"], c["kc"], c["ks"], c["vc"], c["vs"], c["tables"][req], lims,
+                                      np.arange(T + 1), c["sm"])
+    got = oracle.bf16_to_f32(host_bits(out)).astype(np.float64).reshape(want.shape)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    fine = ~np.isnan(want)
+    assert (np.abs(got - want)[fine] <= tol[fine]).all()
+    gl = lse.cpu().numpy().astype(np.float64)
+    live = np.isfinite(wl)
+    assert np.array_equal(live, np.isfinite(gl))
+    assert (np.abs(np.where(live, gl - np.where(live, wl, 0), 0))[live] <= (eps + 2.0 ** -18 * np.abs(np.where(live, wl, 0)))[live]).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,dk,dv", [(8, 2, 128, 128), (4, 4, 64, 64), (3, 3, 192, 128), (16, 1, 64, 64)])
+@pytest.mark.parametrize("lens,new", [([140, 9, 333], [3, 8, 2]), ([9000], [4]), ([300, 200, 129], [300, 140, 1]),
+                                      ([5, 60], [9, 200]), ([700], [520])])
+def test_nan_values_that_a_query_does_not_see(fp8, Hq, Hkv, dk, dv, lens, new):
+    c = _case(lens, new, 16, Hq, Hkv, dk, dv, seed=21)
+    rng = np.random.default_rng(22)
+    for b, (n, m) in enumerate(zip(lens, new)):
+        first = max(0, n - m)
+        for t in {first, n - 1, (first + n) // 2, int(rng.integers(first, n)), int(rng.integers(0, n))}:
+            h, d = int(rng.integers(Hkv)), int(rng.integers(dv))
+            c["vc"][c["tables"][b, t // 16], h, t % 16, d] = 0x7F if t % 2 else 0xFF
+    _check_rows(fp8, c)
