@@ -423,7 +423,8 @@ __device__ __forceinline__ void append_heads(const AppendParams& p, int which, c
     };
     if (infs)
         store(std::integral_constant<int, kDivide>());
-    else if (p.ue8m0)
+    else if (p.ue8m0 && __all_sync(0xFFFFFFFFu, lane >= nh || (__float_as_uint(s) & 0x007FFFFFu) == 0u))
+        // (a page's scale that stays need not be a power of two)
         store(std::integral_constant<int, kUe8m0>());
     else
         store(std::integral_constant<int, kFp32>());

@@ -226,3 +226,27 @@ def test_refusals(fp8):
         fp8.fp8_kv_append(x[..., :64], x[..., :64], sl, kc, ks, vc, vs, scale_fmt=3)
     with pytest.raises(TypeError):
         fp8.fp8_kv_append(x[..., :64].float(), x[..., :64], sl, kc, ks, vc, vs)
+
+
+def test_append_ue8m0_under_scales_that_are_no_powers_of_two(fp8):
+    # Pages written with fp32 scales, appended to in ue8m0: the page's scale stays where it is the larger, and the codes
+    # are e4m3(x / s) for it.  Every bf16 mantissa over the exponents that such a page meets; page maxima of any mantissa.
+    H, d, bs = 64, 128, 16
+    rng = np.random.default_rng(31)
+    bits = np.empty((8, H, d), np.uint16)
+    bits[:] = ((np.arange(8)[:, None, None] + 116) << 7) | np.arange(128)   # 2^-11 .. 2^-4
+    bits |= (rng.random(bits.shape) < 0.5).astype(np.uint16) << 15
+    slots = np.concatenate([np.arange(3, 7), np.arange(16 + 9, 16 + 13)])
+    kc, vc = (syn.random_e4m3_codes((2, H, bs, d), s) for s in (32, 33))
+    tops = oracle.bf16_to_f32((((rng.integers(127, 140, (4, H)) << 7) | rng.integers(0, 128, (4, H))).astype(np.uint16)))
+    tops = np.asarray(tops, np.float32).reshape(4, H)
+    tops[:, 0] = 1104.0
+    scales = tops / np.float32(448)
+    x = oracle.bf16_to_f32(bits).astype(np.float32).reshape(bits.shape)
+    f32 = x[:4] / scales[0][:, None]
+    by_reciprocal = x[:4] * (np.float32(1) / scales[0])[:, None]
+    assert (oracle.e4m3_encode(f32) != oracle.e4m3_encode(by_reciprocal)).any()   # the two ways differ here
+    _check_append(fp8, bits, bits, slots, kc, scales[:2], vc, scales[2:], True)
+    mixed = scales.copy()
+    mixed[:, ::2] = 2.0   # powers of two beside them, in the same warp
+    _check_append(fp8, bits, bits, slots, kc, mixed[:2], vc, mixed[2:], True)
