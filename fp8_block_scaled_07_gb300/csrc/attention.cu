@@ -41,7 +41,8 @@ extern "C" fp8_status fp8_kv_attention(const void* q, int64_t q_token_stride, in
                                        int32_t dk, int32_t dv, float sm_scale, void* out, float* lse, void* workspace,
                                        size_t workspace_bytes, void* stream) {
     if (T < 0 || B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || n_pages <= 0 || width <= 0) return FP8_ERR_INVALID_ARG;
-    if (!block_size_ok(block_size) || static_cast<int64_t>(width) * block_size > (1LL << 31) - 1)
+    // (tiles of 128 tokens, the last one's end included, are counted in 31 bits)
+    if (!block_size_ok(block_size) || static_cast<int64_t>(width) * block_size > (1LL << 31) - 128)
         return FP8_ERR_INVALID_ARG;
     if (!(sm_scale > 0.0f) || std::isinf(sm_scale) || q_token_stride < 0 || q_head_stride < 0 || q_token_stride % 8 || q_head_stride % 8)
         return FP8_ERR_INVALID_ARG;

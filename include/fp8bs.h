@@ -319,7 +319,7 @@ fp8_status fp8_kv_append(const void* k, int64_t k_token_stride, int64_t k_head_s
  * lse of -inf.  Tokens of a page outside the cache, or whose v_scale is not
  * positive, are left out; k_scale may be any finite number.  q row r, head h starts at q + r * q_token_stride +
  * h * q_head_stride (elements; multiples of 8, base 16-byte aligned).
- * out is 32-byte aligned.  (dk, dv) in {(64, 64), (128, 128), (192, 128)},
+ * out is 32-byte aligned, width * block_size <= 2^31 - 128.  (dk, dv) in {(64, 64), (128, 128), (192, 128)},
  * else FP8_ERR_UNSUPPORTED.  Sums and softmax statistics are fp32; the
  * probabilities enter the second product with 9 significant bits or more.
  * (With few rows per request, one below 2^-9 of its row's largest is a

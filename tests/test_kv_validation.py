@@ -88,3 +88,9 @@ def test_attention_workspace(L):
     assert _call(L.fp8_kv_attention, list(ATTEND), ATTEND, ws_bytes=size - 1) == 5
     assert _call(L.fp8_kv_attention, list(ATTEND), ATTEND, ws=None, ws_bytes=0) == 5
     assert isinstance(ctypes.c_size_t(size).value, int)
+
+
+@pytest.mark.parametrize("block,width", [(16, (1 << 27) - 1), (32, (1 << 26) - 1), (64, (1 << 25) - 1), (128, 1 << 24)])
+def test_attention_counts_whole_tiles_in_31_bits(L, block, width):
+    # the last tile of 128 tokens would end past 2^31 - 1
+    assert _call(L.fp8_kv_attention, list(ATTEND), ATTEND, block=block, width=width) == INVALID
