@@ -39,7 +39,7 @@ constexpr float kMostBits = 8.0f;   // and at most 256 with one that has since b
                                     // hi that lo has to hold is 256 there, below e4m3's 448
 constexpr int kThreads = 256;
 constexpr int kJoinThreads = 256;
-constexpr int kNanBits = 8;         // a request of this kernel has at most 128 rows, and so few tokens that only some see
+constexpr int kNanBits = 8;         // a segment's rows are at most 32 queries, and what none of them sees need not be told apart
 
 // A part: O of each row, then (M, l) of each; a multiple of 16 bytes.
 __host__ __device__ constexpr int part_floats(int ru, int dv) { return ru * dv + (ru < 2 ? 4 : 2 * ru); }
@@ -262,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU, kSeveral>::kBlocks)
         int segs = 0, tiles = 0;
         if (b < p.B) {
             const int len = max(0, min(p.lens[b], cap));
-            const int n = p.offsets ? p.offsets[b + 1] - p.offsets[b] : 1;
-            const long long rows = static_cast<long long>(n) * p.G;
+            const int64_t n = p.offsets ? min(static_cast<int64_t>(p.offsets[b + 1] - p.offsets[b]), p.T - p.offsets[b]) : 1;
+            const int64_t rows = n * p.G;   // (q may end before the request)
             s_len[b] = len;
             tiles = (len + 127) >> 7;
             if (len > 0 && rows > 0 && rows <= p.few_rows) segs = (static_cast<int>(rows) + RU - 1) / RU;
@@ -879,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU, kSeveral>::kBlocks)
                         const uint4 v = *chunk(c);
                         if (e4m3_nans(v) == 0) continue;
                         *chunk(c) = without_nans(v);
-                        note_nans(v, s_nan + (sg & 1) * DV + c * 16, nan_key<kNanBits>(sg + 1, tok - least));
+                        note_nans(v, s_nan + (sg & 1) * DV + c * 16, nan_key<kNanBits>(sg + 1, min(tok - least, (1 << kNanBits) - 1)));
                         s_nans[sg & 1] = sg + 1;
                     }
                 }

@@ -280,12 +280,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         long long mine = 0;
         if (b < p.B) {
             const int len = max(0, min(p.lens[b], cap)), first = p.offsets[b], n = p.offsets[b + 1] - first;
-            const long long rows = static_cast<long long>(n) * p.G;
+            const int64_t rows = min(static_cast<int64_t>(n), p.T - first) * p.G;   // (q may end before the request)
             s_len[b] = len;
             s_n[b] = n;
             s_first[b] = first;
-            if (len > 0 && first >= 0 && first + static_cast<int64_t>(n) <= p.T && rows > p.few_rows && rows < (1LL << 31) - 512)
-                mine = (rows + 255) / 256 * p.Hkv;
+            if (len > 0 && first >= 0 && rows > p.few_rows && rows < (1LL << 31) - 512) mine = (rows + 255) / 256 * p.Hkv;
         }
         long long inc = mine;
 #pragma unroll
@@ -341,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m.len = s_len[l];
                 m.n = s_n[l];
                 m.first = s_first[l];
-                m.rows = m.n * p.G;
+                m.rows = static_cast<int>(min(static_cast<int64_t>(m.n), p.T - m.first)) * p.G;
                 const int rem = static_cast<int>(idx - s_cum[l]), at = rem / p.Hkv;
                 m.h = rem - at * p.Hkv;
                 m.row0 = ((m.rows + 255) / 256 - 1 - at) * 256;   // longest first

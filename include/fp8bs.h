@@ -310,8 +310,8 @@ fp8_status fp8_kv_append(const void* k, int64_t k_token_stride, int64_t k_head_s
                          float* v_scale, int64_t n_pages, int32_t block_size, int scale_fmt, void* stream);
 
 /* Attention of T query rows over the cache.  Request b's queries are rows
- * [offsets[b], offsets[b+1]) of q (offsets == NULL: one query per request,
- * T == B), the last n of its lens[b] tokens: query j of n sees tokens
+ * [offsets[b], offsets[b+1]) of q, as far as q goes (offsets == NULL: one
+ * query per request, T == B), the last n of its lens[b] tokens: query j of n sees tokens
  * t < lens[b] - n + j + 1.  Query head h reads cache head h / (Hq / Hkv):
  *   out[row, h] = sum_t softmax_t(sm_scale * q . k_t) v_t   [T, Hq, dv] bf16
  *   lse[row, h] = log sum_t exp(sm_scale * q . k_t)         [T, Hq] fp32 (nullable)

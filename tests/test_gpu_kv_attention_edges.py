@@ -147,3 +147,18 @@ def test_nan_values_that_a_query_does_not_see(fp8, Hq, Hkv, dk, dv, lens, new):
             h, d = int(rng.integers(Hkv)), int(rng.integers(dv))
             c["vc"][c["tables"][b, t // 16], h, t % 16, d] = 0x7F if t % 2 else 0xFF
     _check_rows(fp8, c)
+
+
+# ------------------------------------------------------------------ fewer rows than tokens
+@pytest.mark.parametrize("lens,new,T", [([300, 200], [150, 120], 200), ([300, 200], [150, 120], 120), ([40, 50], [3, 4], 5), ([700], [500], 2),
+                                        ([30, 300, 60], [2, 200, 9], 140)])
+def test_queries_end_inside_a_request(fp8, lens, new, T):
+    c = _case(lens, new, 16, 8, 4, 128, 128, seed=23)
+    want, wl, tol, eps = kv.attention(c["q"], c["kc"], c["ks"], c["vc"], c["vs"], c["tables"], c["lens"], c["offsets"], c["sm"])
+    big = torch.full((T + 40, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T + 40, 8), 7.0, device="cuda")
+    _run(fp8, {**c, "q": c["q"][:T]}, out=big[:T], lse=lse[:T])
+    got = oracle.bf16_to_f32(host_bits(big[:T])).astype(np.float64).reshape(T, 8, 128)
+    assert (np.abs(got - want[:T]) <= tol[:T]).all()
+    assert (np.abs(lse[:T].cpu().numpy() - wl[:T]) <= eps[:T] + 2.0 ** -18 * np.abs(wl[:T])).all()
+    assert (big[T:] == 7.0).all() and (lse[T:] == 7.0).all()
