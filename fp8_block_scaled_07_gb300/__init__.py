@@ -577,9 +577,13 @@ def fp8_kv_attention(q, k_cache, k_scale, v_cache, v_scale, tables, lens, offset
 
 
 def _kv_ws_size(T, B, Hq, Hkv, dk, dv, device):
-    key = ("fp8_kv_attention", T, B, Hq, Hkv, dk, dv, device)
+    """As _ws_size; of T and B only whether they are equal matters (prompts come in every length)."""
+    if T == 0:
+        return 0
+    T = 1 if T == B else 2
+    key = ("fp8_kv_attention", T, Hq, Hkv, dk, dv, device)
     v = _ws_sizes.get(key)
     if v is None:
         with torch.cuda.device(device):
-            v = _ws_sizes[key] = int(lib.fp8_kv_attention_workspace_size(T, B, Hq, Hkv, dk, dv))
+            v = _ws_sizes[key] = int(lib.fp8_kv_attention_workspace_size(T, 1, Hq, Hkv, dk, dv))
     return v

@@ -94,3 +94,14 @@ def test_attention_workspace(L):
 def test_attention_counts_whole_tiles_in_31_bits(L, block, width):
     # the last tile of 128 tokens would end past 2^31 - 1
     assert _call(L.fp8_kv_attention, list(ATTEND), ATTEND, block=block, width=width) == INVALID
+
+
+def test_attention_workspace_sizes_are_kept_by_what_they_depend_on():
+    import fp8_block_scaled_07_gb300 as m
+    seen = len(m._ws_sizes)
+    m._kv_ws_size(5, 0, 8, 4, 128, 128, -1)   # (refused by the call itself)
+    for T in range(1, 300):
+        for B in (1, 7, T):
+            assert m._kv_ws_size(T, B, 8, 4, 128, 128, -1) == m.lib.fp8_kv_attention_workspace_size(T, B, 8, 4, 128, 128)
+    assert len(m._ws_sizes) - seen <= 2
+    assert m._kv_ws_size(0, 3, 8, 4, 128, 128, -1) == 0
