@@ -61,3 +61,36 @@ def test_steps(pa, Hq, Hkv, dk, dv, block):
 def test_command(pa, capsys):
     pa.main(["--layers", "2", "--requests", "3", "--prompt", "40", "--tokens", "3", "--heads", "4", "1", "--width", "256"])
     assert "3 requests, 2 layers" in capsys.readouterr().out
+
+
+def test_one_token_or_one_head_of_odd_rows(pa):
+    # a dimension of one has no stride to be aligned
+    import fp8_block_scaled_07_gb300 as fp8
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((3, 1, 64 * 6 + 4), device="cuda", generator=gen).bfloat16()
+    sl = torch.tensor([16], device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    one = torch.ones(1, **i32)
+
+    def views(y, H):
+        return [y.as_strided((1, n, 64), (388, 64, 1), a) for a, n in ((0, 2 * H), (128, H), (256, H))]
+    for H in (1, 2):
+        q, k, v = views(x, H)   # one token: the rows are 388 values apart
+        assert q.stride(0) % 8
+        res = []
+        for args in ((q, k, v), (q.contiguous(), k.contiguous(), v.contiguous())):
+            cache = fp8.kv_cache(2, H, 16, 64, 64)
+            fp8.fp8_kv_append(args[1], args[2], sl, *cache)
+            out, _ = fp8.fp8_kv_attention(args[0], *cache, one.view(1, 1), one)
+            res.append((cache[0].view(torch.uint8)[1, :, 0], cache[3][1], out))
+        assert all(torch.equal(a, b) for a, b in zip(*res))
+    heads = torch.randn((2, 3, 68), device="cuda", generator=gen).bfloat16()[:, :1, :64]   # one head: 68 values to the next
+    rows = torch.empty((2, 408), dtype=torch.bfloat16, device="cuda")
+    odd = rows[:, :64].unflatten(1, (1, 64)).copy_(heads).as_strided((2, 1, 64), (408, 68, 1))
+    assert odd.stride(1) % 8
+    cache, want = fp8.kv_cache(1, 1, 16, 64, 64), fp8.kv_cache(1, 1, 16, 64, 64)
+    slots = torch.arange(2, device="cuda")
+    fp8.fp8_kv_append(odd, odd, slots, *cache)
+    fp8.fp8_kv_append(heads.contiguous(), heads.contiguous(), slots, *want)
+    assert torch.equal(cache[0].view(torch.uint8)[:, :, :2], want[0].view(torch.uint8)[:, :, :2])
+    fp8.fp8_device_status()
