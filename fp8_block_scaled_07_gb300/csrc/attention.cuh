@@ -89,6 +89,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLoInv = 1.0f / 32.0f;
 constexpr int kRing = 8;            // tiles whose page constants are staged
 
+// Whether a page's scale of V is one: its logarithm and its reciprocal are finite.
+__device__ __forceinline__ bool is_scale(float v) { return v >= 0x1p-126f && v < INFINITY; }
+
 __device__ __forceinline__ void attn_abort(volatile int* abort_flag) {
     *abort_flag = 1;
     atomicExch(&g_attention_status, static_cast<int>(FP8_ERR_TIMEOUT));

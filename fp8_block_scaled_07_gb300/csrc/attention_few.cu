@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, (Few<DK, DV, RU, kSeveral>::kBlocks)
                 break;
             }
             if (i < ntiles) {
-                const bool on = vs > 0.0f;
+                const bool on = is_scale(vs);
                 s_ck[slot * 8 + sub] = on ? ks : 0.0f;
                 s_lv[slot * 8 + sub] = on ? log2f(vs) : -INFINITY;
                 s_iv[slot * 8 + sub] = on ? 1.0f / vs : 0.0f;

@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int slot = g % kRing;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(&cempty[slot], ((g / kRing) & 1) ^ 1, abort_flag)) != 0;
                 if (!ok) break;
-                const bool on = vs > 0.0f;
+                const bool on = is_scale(vs);
                 const bool there = lane < pages_per_tile && i * 128 + lane * bs < m.len;
                 uint32_t dead = __ballot_sync(0xFFFFFFFFu, there && !on);
                 if (__any_sync(0xFFFFFFFFu, there && on && !(ks >= kLeast))) dead |= kOdd;

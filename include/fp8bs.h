@@ -316,8 +316,8 @@ fp8_status fp8_kv_append(const void* k, int64_t k_token_stride, int64_t k_head_s
  *   out[row, h] = sum_t softmax_t(sm_scale * q . k_t) v_t   [T, Hq, dv] bf16
  *   lse[row, h] = log sum_t exp(sm_scale * q . k_t)         [T, Hq] fp32 (nullable)
  * A query that sees no token, and a row past offsets[B], gives zeros and an
- * lse of -inf.  Tokens of a page outside the cache, or whose v_scale is not
- * positive, are left out; k_scale may be any finite number.  q row r, head h starts at q + r * q_token_stride +
+ * lse of -inf.  Tokens of a page outside the cache, or whose v_scale is not a
+ * positive normal number, are left out; k_scale may be any finite number.  q row r, head h starts at q + r * q_token_stride +
  * h * q_head_stride (elements; multiples of 8, base 16-byte aligned).
  * out is 32-byte aligned, width * block_size <= 2^31 - 128.  (dk, dv) in {(64, 64), (128, 128), (192, 128)},
  * else FP8_ERR_UNSUPPORTED.  Sums and softmax statistics are fp32; the

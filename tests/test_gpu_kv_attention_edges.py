@@ -162,3 +162,17 @@ def test_queries_end_inside_a_request(fp8, lens, new, T):
     assert (np.abs(got - want[:T]) <= tol[:T]).all()
     assert (np.abs(lse[:T].cpu().numpy() - wl[:T]) <= eps[:T] + 2.0 ** -18 * np.abs(wl[:T])).all()
     assert (big[T:] == 7.0).all() and (lse[T:] == 7.0).all()
+
+
+# ------------------------------------------------------------------ V's scale has no logarithm or no reciprocal
+def test_scales_of_v_that_are_no_normal_numbers(fp8):
+    for new in ([1, 1], [2, 3], [100, 70]):
+        c = _case([400, 300], new, 32, 8, 2, 128, 128, seed=24)
+        for (b, i), v in (((0, 1), 1e-40), ((0, 12), 3e-39), ((0, 6), np.inf), ((1, 0), np.nan), ((1, 3), -1.0), ((1, 9), 1e-45)):
+            c["vs"][c["tables"][b, i]] = v
+        out, lse = _run(fp8, c, ragged=new[0] > 1)
+        c["vs"] = np.where((c["vs"] >= 2.0 ** -126) & np.isfinite(c["vs"]), c["vs"], 0).astype(np.float32)
+        want, wl, tol, eps = kv.attention(c["q"], c["kc"], c["ks"], c["vc"], c["vs"], c["tables"], c["lens"], c["offsets"], c["sm"])
+        got = oracle.bf16_to_f32(host_bits(out)).astype(np.float64).reshape(want.shape)
+        assert (np.abs(got - want) <= tol).all()
+        assert (np.abs(lse.cpu().numpy() - wl) <= eps + 2.0 ** -18 * np.abs(wl)).all()
