@@ -519,6 +519,11 @@ def fp8_kv_plan(past, new, free_pages, used, tables, block_size, T, lens=None, o
     used_out = torch.empty(1, dtype=torch.int32, device=dev) if used_out is None else _cuda(used_out, "used_out", _I32)
     if lens.numel() != B or offsets.numel() != B + 1 or slots.numel() != T or positions.numel() != T or used_out.numel() != 1:
         raise ValueError("output shape mismatch")
+    if B == 0 and T == 0:   # nothing to launch, but these two have values all the same
+        with torch.cuda.stream(stream):
+            offsets.zero_()
+            used_out.copy_(used.view_as(used_out))
+        return lens, offsets, slots, positions, used_out
     _check("fp8_kv_plan", lib.fp8_kv_plan(_ptr(past), _ptr(new), B, block_size, _ptr(free_pages), free_pages.numel(),
                                           _ptr(used), _ptr(tables), width, _ptr(lens), _ptr(offsets), T, _ptr(slots),
                                           _ptr(positions), _ptr(used_out), _stream(stream)))

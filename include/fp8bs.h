@@ -285,9 +285,9 @@ fp8_status fp8_moe_combine(const void* out, const float* w, const int32_t* pair_
  *   used_out [1]      used[0] + pages taken
  * No result may overlap an input or another result (FP8_ERR_INVALID_ARG), so
  * lengths are kept in two buffers, not updated in place: the call only
- * depends on its inputs, and may be repeated.  B <= 8192,
- * width * block_size < 2^31.  slots (and positions) 16-byte aligned are
- * written with wide stores. */
+ * depends on its inputs, and may be repeated.  B <= 8192 (0, with T == 0:
+ * nothing is written), width * block_size < 2^31.  slots (and positions)
+ * 16-byte aligned are written with wide stores. */
 fp8_status fp8_kv_plan(const int32_t* past, const int32_t* fresh, int32_t B, int32_t block_size,
                        const int32_t* free_pages, int32_t n_free, const int32_t* used, int32_t* tables,
                        int32_t width, int32_t* lens, int32_t* offsets, int64_t T, int64_t* slots,

@@ -250,3 +250,14 @@ def test_append_ue8m0_under_scales_that_are_no_powers_of_two(fp8):
     mixed = scales.copy()
     mixed[:, ::2] = 2.0   # powers of two beside them, in the same warp
     _check_append(fp8, bits, bits, slots, kc, mixed[:2], vc, mixed[2:], True)
+
+
+def test_plan_of_no_requests(fp8):
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    lens, offsets, slots, positions, used = fp8.fp8_kv_plan(
+        none, none, dev_i32([4, 5]), dev_i32([1]), none.view(0, 3), 16, 0,
+        offsets=dev_i32([-7]), used_out=dev_i32([-7]), stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert offsets.tolist() == [0] and used.tolist() == [1] and not (lens.numel() or slots.numel() or positions.numel())
+    with pytest.raises(fp8.Fp8Error):
+        fp8.fp8_kv_plan(none, none, none, dev_i32([0]), none.view(0, 3), 16, 2)   # rows of nobody
