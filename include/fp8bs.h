@@ -302,6 +302,12 @@ fp8_status fp8_kv_plan(const int32_t* past, const int32_t* fresh, int32_t B, int
  *   s = max(act_quant's scale of the new values, the page's scale if it holds
  *       earlier tokens); code = e4m3_rne_satfinite(x / s);
  *   if s grew, the earlier tokens' codes become e4m3_rne((code * s_old) / s).
+ * With fp32 scales each growth rounds the earlier codes once more: after g of
+ * them a value is within a factor (1 + 2^-4)^(g + 1) of what was appended
+ * (subnormal codes aside), and where the scale creeps up by less than half a
+ * code's step at a time, a code stays as it is and its value grows with the
+ * scale.  In ue8m0 a scale grows by powers of two, which the codes follow
+ * exactly: the format for pages that fill token by token.
  * An infinity does not set the scale and is stored as +-448; a NaN is stored
  * as NaN.  dk and dv multiples of 16, at most 1024. */
 fp8_status fp8_kv_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,

@@ -261,3 +261,22 @@ def test_plan_of_no_requests(fp8):
     assert offsets.tolist() == [0] and used.tolist() == [1] and not (lens.numel() or slots.numel() or positions.numel())
     with pytest.raises(fp8.Fp8Error):
         fp8.fp8_kv_plan(none, none, none, dev_i32([0]), none.view(0, 3), 16, 2)   # rows of nobody
+
+
+@pytest.mark.parametrize("ue8m0", [False, True])
+def test_append_token_by_token_under_growing_scales(fp8, ue8m0):
+    H, d, bs, n = 3, 64, 64, 50
+    rng = np.random.default_rng(41)
+    x = syn.to_bf16_bits((rng.standard_normal((n, H, d)) * (1.03 ** np.arange(n))[:, None, None]).astype(np.float32))
+    kc, ks, vc, vs = fp8.kv_cache(2, H, bs, d, d)
+    kc.view(torch.uint8).zero_()
+    vc.view(torch.uint8).zero_()
+    c, s = np.zeros((2, H, bs, d), np.uint8), np.zeros((2, H), np.float32)
+    t = dev_bf16(x)
+    for i in range(n):
+        fp8.fp8_kv_append(t[i:i + 1], t[i:i + 1], torch.tensor([bs + i], device="cuda"), kc, ks, vc, vs,
+                          scale_fmt=fp8.FP8_SCALE_UE8M0 if ue8m0 else fp8.FP8_SCALE_FP32)
+        c, s = kv.append(x[i:i + 1], np.array([bs + i]), c, s, ue8m0)
+        assert np.array_equal(host_bits(kc), c) and np.array_equal(host_bits(vc), c), i
+        assert np.array_equal(host_f32(ks), s)
+    fp8.fp8_device_status()

@@ -64,3 +64,26 @@ def test_attention_rows_with_nothing_to_see():
                                   np.array([0, 3, 4]), 0.125)
     assert not out[0].any() and lse[0, 0] == -np.inf and not out[3].any() and lse[3, 0] == -np.inf
     assert out[1].any() and np.isfinite(lse[2, 0])
+
+
+def test_append_errors_after_many_growths():
+    # one token after the other, each a little larger than the last: the bounds that the header states
+    n, d = 64, 64
+    rng = np.random.default_rng(7)
+    f = (rng.uniform(1.0, 2.0, (n, 1, d)) * np.sign(rng.standard_normal((n, 1, d)))).astype(np.float32)
+    f *= (1.03 ** np.arange(n))[:, None, None].astype(np.float32)
+    x = syn.to_bf16_bits(f)
+    f = oracle.bf16_to_f32(x).astype(np.float64).reshape(n, d)
+    for ue8m0 in (False, True):
+        c, s = np.zeros((1, 1, n, d), np.uint8), np.zeros((1, 1), np.float32)
+        grown, low = np.zeros(n), np.zeros(n)   # growths since a token was appended; what subnormal codes may have lost
+        for i in range(n):
+            was = s[0, 0]
+            c, s = kv.append(x[i:i + 1], np.arange(i, i + 1), c, s, ue8m0)
+            if s[0, 0] > was:
+                grown[:i] += 1
+                low[:i] += s[0, 0] * 2.0 ** -10
+        assert grown[0] >= (2 if ue8m0 else 30)
+        got = oracle.e4m3_decode(c[0, 0]).astype(np.float64).reshape(n, d) * float(s[0, 0])
+        bound = np.abs(f) * (2.0 ** -4 if ue8m0 else ((1 + 2.0 ** -4) ** (grown + 1) - 1)[:, None]) + low[:, None] + s[0, 0] * 2.0 ** -10
+        assert (np.abs(got - f) <= bound * (1 + 1e-6)).all()
