@@ -489,17 +489,12 @@ def _rows(t, name):
     return t
 
 
-def _steps(t):
-    """Token and head strides; 0 of a dimension of one, whose stride leads nowhere and may be any number."""
-    ts, hs, _ = t.stride()
-    return ts if t.shape[0] > 1 else 0, hs if t.shape[1] > 1 else 0
-
-
 def fp8_kv_plan(past, new, free_pages, used, tables, block_size, T, lens=None, offsets=None, slots=None,
                 positions=None, used_out=None, stream=None):
     """Block tables and slot maps of one step.  past, new int32 [B]; free_pages
     int32 [F], of which used[0] are taken; tables int32 [B, width], completed
-    in place; T token rows.  No other result may share memory with an input
+    in place; T token rows.  Free pages go to the requests in their order, up
+    to the first that they do not cover.  No other result may share memory with an input
     (lens with past, used_out with used).  Returns (lens [B], offsets [B+1], slots [T] int64,
     positions [T] int32, used_out [1])."""
     _cuda(past, "past", _I32, 1)
@@ -540,8 +535,12 @@ def fp8_kv_append(k, v, slots, k_cache, k_scale, v_cache, v_scale, scale_fmt=FP8
     T = slots.numel()
     if k.shape != (T, H, dk) or v.shape != (T, H, dv):
         raise ValueError("shape mismatch")
-    kts, khs = _steps(k)
-    vts, vhs = _steps(v)
+    kts, khs, _ = k.stride()
+    vts, vhs, _ = v.stride()
+    if T == 1:   # (the stride of a dimension of one leads nowhere, and may be any number)
+        kts = vts = 0
+    if H == 1:
+        khs = vhs = 0
     _check("fp8_kv_append", lib.fp8_kv_append(
         k.data_ptr(), kts, khs, v.data_ptr(), vts, vhs, slots.data_ptr(), T, H, dk, dv, k_cache.data_ptr(),
         k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(), P, bs, int(scale_fmt), _stream(stream)))
@@ -576,7 +575,11 @@ def fp8_kv_attention(q, k_cache, k_scale, v_cache, v_scale, tables, lens, offset
     if workspace is None:
         dev = q.get_device()
         workspace = workspaces.get(_kv_ws_size(T, B, Hq, H, dk, dv, dev), dev, st)
-    ts, hs = _steps(q)
+    ts, hs, _ = q.stride()
+    if T == 1:   # (as in fp8_kv_append)
+        ts = 0
+    if Hq == 1:
+        hs = 0
     status = lib.fp8_kv_attention(
         q.data_ptr(), ts, hs, k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(), P, bs,
         tables.data_ptr(), width, lens.data_ptr(), _ptr(offsets), B, T, Hq, H, dk, dv,

@@ -80,9 +80,10 @@ extern "C" fp8_status fp8_kv_attention(const void* q, int64_t q_token_stride, in
     // spreads it over the GPU; the many-rows kernel once for 256 rows, on one
     // SM for each of them and each cache head.  So a request stays with the
     // former for two passes (64 requests of 4096 tokens, 8 cache heads of 128:
-    // 16 rows 112 us, 32 rows 209, 40 rows 304; the other kernel 189 for all),
-    // and for four where the latter could not fill the GPU (4 requests: 32 rows
-    // 23 us, 64 rows 36, 128 rows 55; the other kernel 57).
+    // 16 rows 113 us, 32 rows 210, where a third pass would make it 304; the
+    // other kernel 198 to 202 for 40 to 128 rows, so that two passes are about
+    // even with it), and for four where the latter could not fill the GPU (4
+    // requests: 32 rows 27 us, 64 rows 36, 128 rows 58; the other kernel 71).
     p.few_rows = offsets ? (static_cast<int64_t>(B) * Hkv < sms ? 4 : 2) * ru : G;
     // maps over [n_pages][Hkv * block_size] rows
     const int64_t rows = static_cast<int64_t>(Hkv) * block_size;

@@ -19,7 +19,8 @@ from . import (fp8_device_status, fp8_kv_append, fp8_kv_attention, fp8_kv_plan, 
 
 
 class Requests:
-    """The requests' lengths, block tables and free pages, on the device."""
+    """The requests' lengths, block tables and free pages, on the device.
+    Pages are handed out and not taken back: a finished request keeps its own."""
 
     def __init__(self, n_requests, n_pages, block_size, max_len, device="cuda"):
         def i32(*shape):
@@ -33,8 +34,9 @@ class Requests:
     def step(self, new, T):
         """Pages and slots for new [B] int32 tokens of each request, T rows in
         all.  Returns the step's (offsets, slots, positions).  A request that
-        the free pages or its table's width do not cover keeps its length, and
-        its rows have slot -1."""
+        its table's width or the free pages do not cover keeps its length, and
+        its rows have slot -1; the first that the free pages do not cover ends
+        their handing out for the step."""
         _, offsets, slots, positions, _ = fp8_kv_plan(
             self.lens, new, self.free_pages, self.used, self.tables, self.block_size, T, lens=self._lens2,
             used_out=self._used2)
@@ -45,7 +47,9 @@ class Requests:
 
 class PagedAttention:
     """One layer.  wqkv [(Hq + Hkv) dk + Hkv dv, D] and wo [D, Hq dv]: e4m3 with
-    128 x 128 block scales (fp8_weight_quant), Q's heads first, then K's, then V's."""
+    128 x 128 block scales (fp8_weight_quant), Q's heads first, then K's, then V's.
+    Without a rotary embedding: its place is between project and the append, by
+    the plan's positions."""
 
     def __init__(self, wqkv, wqkv_s, wo, wo_s, Hq, Hkv, dk, dv, n_pages, block_size):
         if wqkv.shape[0] != (Hq + Hkv) * dk + Hkv * dv or wo.shape[1] != Hq * dv:

@@ -256,9 +256,9 @@ fp8_status fp8_moe_quant_scatter(const void* x, const int32_t* pair_row, int64_t
 fp8_status fp8_moe_combine(const void* out, const float* w, const int32_t* pair_row, int64_t T,
                            int32_t topk, int64_t D, void* y_bf16, float* y_fp32, void* stream);
 
-/* ---- The paged 8-bit key/value cache between the projections (the pages
- * keep K and V in bf16 caches; this is the 8-bit form of the same cache, one
- * scale per page and head, in the convention of act_quant's blocks).
+/* ---- The paged 8-bit key/value cache between the projections: K and V as
+ * e4m3 codes, with one scale per page of the cache and head, by act_quant's
+ * rule for a block.
  *
  * A page holds block_size tokens (16, 32, 64 or 128) of all H heads:
  *   k_cache [n_pages, H, block_size, dk] e4m3, k_scale [n_pages, H] fp32, and
@@ -276,7 +276,11 @@ fp8_status fp8_moe_combine(const void* out, const float* w, const int32_t* pair_
  * The pages it needs beyond those of its past are taken from free_pages
  * [n_free], starting at entry used[0], in request order, and written to its
  * row of `tables` (other entries stay).  A request whose new length does not
- * fit its row, or whose pages the free list no longer has, gets none:
+ * fit its row gets none.  The free list is shared out first come, first
+ * served: once a request needs more pages than are left, it gets none, and
+ * nor does any later one that needs a page, a smaller one included (the
+ * order of the requests decides, so that a large one is not passed over for
+ * good); later requests that stay within their last page go on:
  *   lens [B]          past + fresh, or past for a request that got none
  *   offsets [B + 1]   running sum of fresh: rows of the step's tokens
  *   slots [T]         int64, the slot of each token row; -1 for tokens of a
