@@ -7,7 +7,8 @@
 //   out[j]  = sum_t softmax_t(S[j, t]) * v_code[t] * v_scale[page(t), h]
 // over the tokens t < len - n + j + 1 of the request (j counts its n queries;
 // its last query sees the whole cache).  A query that sees nothing gives
-// zeros, and an lse of -inf.
+// zeros, and an lse of -inf.  What a query does not see has no part in its
+// result, a NaN in K (masked after the product) or in V (note_nans) neither.
 //
 // Both products run on the tensor core: the e4m3 bytes go from HBM by TMA into
 // shared memory.  K is read there by tcgen05.mma as it is, and so is V for few

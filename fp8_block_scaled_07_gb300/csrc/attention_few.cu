@@ -50,7 +50,10 @@ __host__ __device__ constexpr int info_ints(int ru) { return 4 + (ru < 2 ? 4 : 2
 __host__ __device__ constexpr int few_blocks(int ru) { return ru > 16 ? 1 : 2; }
 
 // RU: the rows that are computed; the MMA has at least NR = 8.  kSeveral: a
-// request may have several queries, and then tokens that only some rows see.
+// request may have several queries, and then tokens that only some rows see,
+// whose V is looked over for NaNs.  (Kernels of their own: with the search in
+// those of single tokens too, 8 rows of 64 values took 69.5 us against 66.8,
+// 32 rows of 128 62.5 against 60.6.)
 template <int DK, int DV, int RU, bool kSeveral>
 struct Few {
     static constexpr int NR = RU < 8 ? 8 : RU;

@@ -34,12 +34,13 @@
 // Each row tile has an issuing warp of its own, and that warp runs as a whole
 // (see warp_mma_e4m3).
 //
-// 128 tokens for 256 rows take 1.72 us with dk = 128 (1.29 us is what the
-// products take alone, 2480 cycles) and 1.99 us with dk = 192 (1.73 us); a
-// call has some 13 us more for its start, first loads and last results.
-//   prompt of 4096, 128 heads of 192/128: 535 us, 1285 TFLOP/s (tensor pipe 58% busy)
-//   chunks of 2048, 1437 and 1552 with a past, 32 heads on 8 of 128: 202 us, 1033 TFLOP/s
+// 128 tokens for 256 rows take 1.73 us with dk = 128 (1.29 us is what the
+// products take alone, 2480 cycles) and 2.01 us with dk = 192 (1.73 us); a
+// call has some 21 us more for its start, first loads and last results.
+//   prompt of 4096, 128 heads of 192/128: 572 us, 1201 TFLOP/s (tensor pipe 56% busy)
+//   chunks of 2048, 1437 and 1552 with a past, 32 heads on 8 of 128: 201 us, 1040 TFLOP/s
 //   (640 items on 152 SMs: 9% of the time is the last round's)
+// (in a long run of calls; under a profiler, cold, the prompt takes 538 us)
 #include "attention.cuh"
 
 namespace fp8bs {
