@@ -187,7 +187,11 @@ class _Workspace:
         with self._lock:
             buf = self._bufs.get(key)
             if buf is None or buf.numel() < nbytes:
-                buf = torch.zeros(max(nbytes, 1 << 16), dtype=torch.uint8, device=torch.device("cuda", device))
+                # (on the call's stream, which need not be the current one: it is filled before the call uses it,
+                # and the one it replaces is handed out again after the calls that used that)
+                with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream else
+                                       torch.cuda.default_stream(device)):
+                    buf = torch.zeros(max(nbytes, 1 << 16), dtype=torch.uint8, device=torch.device("cuda", device))
                 self._bufs[key] = buf
             return buf
 

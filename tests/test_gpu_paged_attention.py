@@ -94,3 +94,36 @@ def test_one_token_or_one_head_of_odd_rows(pa):
     fp8.fp8_kv_append(heads.contiguous(), heads.contiguous(), slots, *want)
     assert torch.equal(cache[0].view(torch.uint8)[:, :, :2], want[0].view(torch.uint8)[:, :, :2])
     fp8.fp8_device_status()
+
+
+def test_workspace_is_filled_on_the_calls_stream(pa):
+    # A call on a stream of its own, while the current stream has long work: the workspace it gets first is zero when
+    # the call uses it, though the memory held something else and a fill on the current stream would come too late.
+    import fp8_block_scaled_07_gb300 as fp8
+    n, d, H = 700, 128, 40
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cache = fp8.kv_cache(n // 64 + 1, H, 64, d, d)
+    for codes, scale in (cache[:2], cache[2:]):
+        codes.copy_(torch.randn(codes.shape, device="cuda", generator=gen).to(codes.dtype))
+        scale.fill_(1.0)
+    q = torch.randn((n, H, d), device="cuda", generator=gen).bfloat16()
+    tables = torch.arange(n // 64 + 1, **i32).view(1, -1)
+    args = (q, *cache, tables, torch.tensor([n], **i32))
+    offsets, want = torch.tensor([0, n], **i32), torch.empty_like(q)
+    fp8.fp8_kv_attention(*args, offsets=offsets, out=want)
+    for _ in range(3):
+        s = torch.cuda.Stream()
+        out = torch.zeros_like(q)
+        size = fp8.lib.fp8_kv_attention_workspace_size(n, 1, H, H, d, d)
+        for pool in (torch.cuda.current_stream(), s):
+            with torch.cuda.stream(pool):
+                dirt = [torch.full((max(size, 1 << 16),), 1, dtype=torch.uint8, device="cuda") for _ in range(3)]
+                del dirt
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        fp8.fp8_kv_attention(*args, offsets=offsets, out=out, stream=s)
+        s.synchronize()
+        assert torch.equal(out, want)
+        torch.cuda.synchronize()
+    fp8.fp8_device_status()
